@@ -1,0 +1,62 @@
+"""GPU tests of the autograd functions over 8-bit checkpoints: which gradients they give or
+refuse, the types they take under autocast, and what a captured step records."""
+import ctypes
+
+import pytest
+
+from test_gpu_groups import B, L, tokens, torch  # noqa: F401  (fixtures and helpers)
+
+pytestmark = pytest.mark.gpu
+
+KERNEL, MEMSET = 0, 2    # hipGraphNodeType
+
+
+def node_types(B, graph):
+    """Types of the nodes of a torch.cuda.CUDAGraph that keeps its graph."""
+    hip = B.lib()
+    handle, count = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert hip.hipGraphGetNodes(handle, None, ctypes.byref(count)) == 0
+    nodes = (ctypes.c_void_p * count.value)()
+    assert hip.hipGraphGetNodes(handle, nodes, ctypes.byref(count)) == 0
+    kinds = []
+    for n in nodes:
+        kind = ctypes.c_int(-1)
+        assert hip.hipGraphNodeGetType(ctypes.c_void_p(n), ctypes.byref(kind)) == 0
+        kinds.append(kind.value)
+    return kinds
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("m,n", [(50000, 48), (8192, 1024), (3, 5)])
+def test_bias_alone_in_a_graph(torch, B, dtype, m, n):
+    """A frozen weight under a trained bias: the captured step clears no memory by a memset
+    node, and every replay gives the eager gradient."""
+    from integer_quantized_nn_amd import checkpoint as C
+    dt = getattr(torch, dtype)
+    x, w = tokens(torch, m, 64, dt, 1).cuda(), tokens(torch, n, 64, dt, 2).cuda()
+    dy = tokens(torch, m, n, dt, 3).cuda()
+    b0 = torch.zeros(n, device="cuda", dtype=dt)
+
+    def step(b):
+        return torch.autograd.grad(C.linear(x, w, b), b, dy)[0]
+
+    held = b0.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        out = step(held)
+    kinds = node_types(B, graph)
+    assert KERNEL in kinds and MEMSET not in kinds, kinds
+    for i in range(4):
+        dy.copy_(tokens(torch, m, n, dt, 10 + i))
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(got, step(b0.clone().requires_grad_()))
+        u = torch.finfo(dt).eps / 2
+        want, mag = dy.double().sum(0), dy.double().abs().sum(0)
+        assert ((got.double() - want).abs() <= (m + 4) * 2.0 ** -23 * mag + u * want.abs()).all()
