@@ -13,6 +13,7 @@ import ctypes
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -278,6 +279,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _no_gradient(x, what):
+    """Refuses an x that asks for a derivative, in either mode, of a call that has none."""
+    if (x.requires_grad and torch.is_grad_enabled()) or (
+            forward_ad._current_level >= 0 and forward_ad.unpack_dual(x).tangent is not None):
+        raise ValueError("%s has no gradient" % what)
+
+
 def _done(status):
     if status:
         B._check(status)
@@ -366,7 +374,8 @@ class W4Linear:
         # one token is short of host time: the ordinary call takes as few steps as it can
         if (out is None and stream is None and type(x) is torch.Tensor and x.dtype is self.dtype
                 and x.device == self.device and x.dim() and x.shape[-1] == self.in_features and x.is_contiguous()
-                and not x.requires_grad and torch._C._cuda_getDevice() == self.device.index):
+                and not x.requires_grad and forward_ad._current_level < 0
+                and torch._C._cuda_getDevice() == self.device.index):
             n, k = self.out_features, self.in_features
             y = x.new_empty(x.shape[:-1] + (n,))
             status = self._fwd(self._desc, x.numel() // k, x.data_ptr(), k, self._packed, self._bias, y.data_ptr(), n,
@@ -381,7 +390,7 @@ class W4Linear:
         if _away(dev, stream):
             with _on(dev, stream, x, out, self.packed, self.bias):
                 return self(x, out)
-        _need(not (x.requires_grad and torch.is_grad_enabled()), "W4Linear has no gradient: call it under no_grad()")
+        _no_gradient(x, "W4Linear")
         xr, ld = _rows(x, rows, cols)
         y = _out(out, x.shape[:-1] + (n,), self.dtype, dev, x, self.packed, self.bias)
         B.iqnn_w4_fwd(self.desc, rows, xr, ld, self.packed, self.bias, y, n, _current(dev))
@@ -390,8 +399,10 @@ class W4Linear:
 
 def ckpt_act(x, act, group=128, gated=False, out=None, stream=None):
     """(y, codes, scale): y = act(x), or act(a) * b with x = [a | b] when gated, and the
-    8-bit codes and scales of x that ckpt_act_bwd reads, all from one pass over x."""
+    8-bit codes and scales of x that ckpt_act_bwd reads, all from one pass over x.  No
+    gradient flows through it: checkpoint.act is the function that has one."""
     rows, width, ft = _gpu(x, "x")
+    _no_gradient(x, "ckpt_act (checkpoint.act has)")
     dev = x.device
     if _away(dev, stream):
         with _on(dev, stream, x, out):

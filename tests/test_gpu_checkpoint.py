@@ -60,3 +60,23 @@ def test_bias_alone_in_a_graph(torch, B, dtype, m, n):
         u = torch.finfo(dt).eps / 2
         want, mag = dy.double().sum(0), dy.double().abs().sum(0)
         assert ((got.double() - want).abs() <= (m + 4) * 2.0 ** -23 * mag + u * want.abs()).all()
+
+
+def test_gradients_are_not_dropped(torch, L, B):
+    """Calls without a derivative refuse an input that asks for one, in either mode."""
+    from torch.autograd import forward_ad
+    x = tokens(torch, 4, 64, torch.float32, 1).cuda()
+    w = L.quantize_groups(x, B.INT4, group=32)
+    lin = L.W4Linear(w[0], w[1], group=32, dtype=torch.float32)
+    a = x.clone().requires_grad_()
+    for call in (lambda v: lin(v), lambda v: L.ckpt_act(v, B.ACT_GELU)):
+        with pytest.raises(ValueError, match="gradient"):
+            call(a)
+        with torch.no_grad():
+            call(a)
+        with torch.inference_mode():
+            call(x)
+        with forward_ad.dual_level():
+            call(x)
+            with pytest.raises(ValueError, match="gradient"):
+                call(forward_ad.make_dual(x, torch.ones_like(x)))
