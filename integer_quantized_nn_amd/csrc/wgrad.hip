@@ -27,8 +27,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 //          type -- the activation as it was before it was saved, up to the code's own
 //          half step (2^-8 of the group's maximum; the rounding is 2^-9 or 2^-12 of x^).
 //   SPLIT  f32 gradients: both operands as exact sums of bf16 pieces of 8 significand
-//          bits (dY 1, 2 or 3 of them, x^ 3); products of pieces i + j < 3 are kept, the
-//          others lie below 2^-24 of the product.
+//          bits (dY 1, 2 or 3 of them, x^ 3); products of pieces i + j < 3 are kept.  Where
+//          that leaves any out, pieces are rounded to nearest: piece 1 is at most 2^-8 of the
+//          value and piece 2 2^-17, so what is left out lies below 1.01 * 2^-24 of the product,
+//          of either sign.  (Cut off towards zero it reaches 2^-21, always of the product's
+//          sign; 4096 x 2048 x 2048 f32, group 32: 286 us so, 298 us to nearest.)
 //   FOLD   f32 gradients where a tile's columns share one scale per row: the codes alone
 //          are exact in one piece, and three pieces of dY * s, rounded to binary32 first,
 //          need three products instead of five (f16) or six (f32).
@@ -38,6 +41,7 @@ struct Mode {
     static constexpr int pa = !SPLIT ? 1 : (FOLD || sizeof(T) == 4 ? 3 : (std::is_same<T, _Float16>::value ? 2 : 1));
     static constexpr int pb = SPLIT && !FOLD ? 3 : 1;
     static constexpr bool f16 = !SPLIT && std::is_same<T, _Float16>::value;
+    static constexpr bool nearest = pa > 1 && pb > 1;   // some products of pieces are left out
 };
 
 template <bool F16>
@@ -48,19 +52,34 @@ __device__ __forceinline__ f32x4 mma(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// P bf16 pieces of eight floats, each the truncated upper half of what is left (of an
-// infinity, NaN: a non-finite operand makes its sums non-finite).
-template <int P>
+// P bf16 pieces of eight floats whose sum they are (of an infinity, NaN: a non-finite operand
+// makes its sums non-finite).  Each is the upper half of what is left, or with NEAREST, but for
+// the last, what is left rounded; there the first is kept from rounding up to infinity.
+template <int P, bool NEAREST>
 __device__ __forceinline__ void split8(float v[8], uint4 o[P]) {
+    constexpr float kMax = 0x1.FEp127f;   // bf16's largest
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         uint32_t w[4];
+        if (NEAREST && i + 1 < P) {
+            bf16x8 a;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(as_u32(v[2 * j + 1]), as_u32(v[2 * j]), 0x07060302u);
-        o[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (i + 1 < P) {
+            for (int j = 0; j < 8; ++j) a[j] = (__bf16)(i == 0 ? __builtin_amdgcn_fmed3f(v[j], -kMax, kMax) : v[j]);
+            o[i] = __builtin_bit_cast(uint4, a);
+            w[0] = o[i].x; w[1] = o[i].y; w[2] = o[i].z; w[3] = o[i].w;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = v[j] - as_f32(as_u32(v[j]) & 0xFFFF0000u);
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = v[2 * j] - as_f32(w[j] << 16);
+                v[2 * j + 1] = v[2 * j + 1] - as_f32(w[j] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(as_u32(v[2 * j + 1]), as_u32(v[2 * j]), 0x07060302u);
+            o[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (i + 1 < P) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] - as_f32(as_u32(v[j]) & 0xFFFF0000u);
+            }
         }
     }
 }
@@ -185,7 +204,7 @@ __global__ __launch_bounds__(256 * KS, KS) void wgrad_kernel(const WgradParams p
                     for (int j = 0; j < 8; ++j) v[j] = v[j] * sc;
                 }
                 uint4 o[PA];
-                split8<PA>(v, o);
+                split8<PA, Md::nearest>(v, o);
 #pragma unroll
                 for (int i = 0; i < PA; ++i) *reinterpret_cast<uint4*>(dst + i * BN * kStepM * 2) = o[i];
             } else {
@@ -204,7 +223,7 @@ __global__ __launch_bounds__(256 * KS, KS) void wgrad_kernel(const WgradParams p
             }
             if constexpr (SPLIT && !FOLD) {
                 uint4 o[PB];
-                split8<PB>(v, o);
+                split8<PB, Md::nearest>(v, o);
 #pragma unroll
                 for (int i = 0; i < PB; ++i) *reinterpret_cast<uint4*>(dst + i * BK * kStepM * 2) = o[i];
             } else {
@@ -463,7 +482,7 @@ __global__ __launch_bounds__(256 * KS, 2) void wgrad_ring_kernel(const WgradPara
         uint8_t* dst = xb + (u % XB * KS + ks) * kX + lds_off<BK>(rx + 16 * h, cx);
         if constexpr (SPLIT) {
             uint4 o[PB];
-            split8<PB>(v, o);
+            split8<PB, Md::nearest>(v, o);
 #pragma unroll
             for (int i = 0; i < PB; ++i) *reinterpret_cast<uint4*>(dst + i * BK * kStepM * 2) = o[i];
         } else {
