@@ -192,7 +192,7 @@ struct Unit {
     bool in;
 };
 __device__ __forceinline__ Unit unit_of(int64_t rows, int32_t per_row) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = block_id() * 256 + threadIdx.x;
     Unit r;
     if (rows * per_row < ((int64_t)1 << 31)) {
         r.row = (uint32_t)t / (uint32_t)per_row;
@@ -246,7 +246,7 @@ __device__ __forceinline__ void merge_row(Range& r) {
 template <typename T, bool ASYM, bool FOUR, bool VEC, int WAVES>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const GroupQuantParams p) {
     constexpr int kStep = WAVES * 64 * 8;
-    const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + threadIdx.x / (64 * WAVES);
+    const int64_t row = block_id() * (4 / WAVES) + threadIdx.x / (64 * WAVES);
     if (row >= p.rows) return;   // whole waves; with WAVES = 4 the whole block
     const int64_t t0 = (int64_t)(threadIdx.x % (64 * WAVES)) * 8;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(256) void act_fwd_groups_kernel(const ActParams p) 
 template <typename T, bool GATED, bool VEC, int WAVES>
 __global__ __launch_bounds__(256) void act_fwd_rows_kernel(const ActParams p) {
     constexpr int kStep = WAVES * 64 * 8;
-    const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + threadIdx.x / (64 * WAVES);
+    const int64_t row = block_id() * (4 / WAVES) + threadIdx.x / (64 * WAVES);
     if (row >= p.rows) return;   // whole waves; with WAVES = 4 the whole block
     const int64_t t0 = (int64_t)(threadIdx.x % (64 * WAVES)) * 8;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
@@ -531,12 +531,7 @@ hipError_t with_bool(bool b, F f) {
     return b ? f(std::true_type()) : f(std::false_type());
 }
 
-hipError_t blocks_of(int64_t threads, dim3* g) {
-    const int64_t b = (threads + 255) / 256;
-    if (b > 0x7FFFFFFF) return hipErrorInvalidValue;
-    *g = dim3((unsigned)b);
-    return hipSuccess;
-}
+hipError_t blocks_of(int64_t threads, dim3* g) { return grid_of((threads + 255) / 256, 256, g); }
 
 }  // namespace
 

@@ -192,6 +192,17 @@ hipError_t launch_maxpool(const PoolParams& p, hipStream_t stream);
 
 // ---- group-scaled codes (group_quant.hip, w4.hip, wgrad.hip, group_api.cpp) -----------
 
+// Grid of `blocks` blocks of `threads` threads.  A launch holds fewer than 2^32 threads along
+// one axis; more blocks stand in several rows of y, counted through by block_id(), where up to
+// one block a row lies past the end.
+inline hipError_t grid_of(int64_t blocks, int threads, dim3* g) {
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int64_t most = 0xFFFFFFFFll / threads, rows = (blocks + most - 1) / most;
+    *g = dim3((unsigned)((blocks + rows - 1) / rows), (unsigned)rows);
+    return hipSuccess;
+}
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Floating-point element types and activations, same numbering as iqnn_ftype, iqnn_act.
 enum : int32_t { F_F32 = 0, F_F16 = 1, F_BF16 = 2 };
 enum : int32_t { A_RELU = 0, A_GELU = 1, A_GELU_TANH = 2, A_SILU = 3 };

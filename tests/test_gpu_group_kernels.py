@@ -107,3 +107,31 @@ def test_wgrad_pieces_of_the_largest_and_of_infinities(torch, L, dtype, n, k):
     s[r, 1] = float("inf")
     dw, _ = L.ckpt_wgrad(dy, q, s, group=32, out_dtype=torch.float32)
     assert not torch.isfinite(dw[:, 32:64]).any() and torch.isfinite(dw[:, :32]).all() and torch.isfinite(dw[:, 64:]).all()
+
+
+# ------------------------------------------------ launches of 2^32 threads and more
+
+def halves_equal(torch, call, whole, rows, *inputs):
+    """Every output of `call` on all rows is that of its two halves, which stay below 2^32
+    threads a launch."""
+    half = rows // 2
+    for lo, hi in ((0, half), (half, rows)):
+        for a, b in zip(whole, call(*[t[lo:hi] for t in inputs])):
+            assert torch.equal(a[lo:hi], b)
+
+
+@pytest.mark.parametrize("rows,cols,group", [((1 << 26) + 3, 16, 0), ((1 << 28) + 3, 1, 128)])
+def test_group_codes_past_a_launch(torch, L, B, rows, cols, group):
+    """A wave for each of 2^26 rows, and 16 threads for each of 2^28."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    quant = lambda v: L.quantize_groups(v, B.INT8, group=group)[:2]
+    q, s = quant(x)
+    halves_equal(torch, quant, (q, s), rows, x)
+    back = lambda a, b: (L.dequantize_groups(a, b, None, B.INT8, group=group, dtype=torch.bfloat16),)
+    halves_equal(torch, back, back(q, s), rows, q, s)
+    act = lambda v: L.ckpt_act(v, B.ACT_GELU, group=group)
+    y, aq, sa = act(x)
+    halves_equal(torch, act, (y, aq, sa), rows, x)
+    grad = lambda d, a, b: (L.ckpt_act_bwd(d, a, b, B.ACT_GELU, group=group),)
+    halves_equal(torch, grad, grad(y, aq, sa), rows, y, aq, sa)
