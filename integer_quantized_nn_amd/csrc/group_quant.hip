@@ -515,7 +515,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const ActParams p) {
 
 // ---- launch -------------------------------------------------------------------------
 
-// A row whose 8-element units exceed this many is shared by the four waves of a block.
+// A row of more elements than this is shared by the four waves of a block.
 constexpr int64_t kWaveRow = 4 * 64 * 8;
 
 template <typename F>
