@@ -243,7 +243,7 @@ __global__ __launch_bounds__(W * 64) void w4_few_kernel(const W4Params p) {
     constexpr int C = 16 / ML, X = 4 / C, R = 4 / C;   // loads of x per block; accumulator registers of distinct rows
     __shared__ float red[W][NT][R * 64];
     const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, i = l & 15, g = l >> 4;
-    const int64_t t0 = (int64_t)blockIdx.x * NT;
+    const int64_t t0 = block_id() * NT;   // a block past the end repeats the last rows and stores nothing
     const uint4* codes[NT];
     const float* sc[NT];
     const uint8_t* zc[NT];
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : KS) void w4_tile_kernel(con
     // consecutive blocks go to the eight XCDs in turn: each XCD takes a run of tiles that
     // share their weights
     const int64_t mblk = (p.m + 16 * MT - 1) / (16 * MT);
-    const uint32_t G = gridDim.x, q8 = G / 8, r8 = G % 8, xcd = blockIdx.x % 8;
-    const int64_t tile = (int64_t)(xcd < r8 ? xcd * (q8 + 1) : r8 * (q8 + 1) + (xcd - r8) * q8) + blockIdx.x / 8;
+    const uint32_t G = gridDim.x * gridDim.y, q8 = G / 8, r8 = G % 8, id = (uint32_t)block_id(), xcd = id % 8;
+    const int64_t tile = (int64_t)(xcd < r8 ? xcd * (q8 + 1) : r8 * (q8 + 1) + (xcd - r8) * q8) + id / 8;
     const int64_t m0 = (tile % mblk) * 16 * MT, t0 = (tile / mblk) * 4 * NT + wave * NT;
 
     const uint4* codes[NT];
@@ -524,16 +524,18 @@ template <typename T, bool ASYM, int GPB, bool VEC>
 hipError_t launch_rows(const W4Params& p, hipStream_t stream) {
     const auto few = [&](auto ml, auto nt, auto w, auto u) {
         constexpr int ML = decltype(ml)::value, NT = decltype(nt)::value, W = decltype(w)::value, U = decltype(u)::value;
-        const int64_t blocks = (p.g.nt + NT - 1) / NT;
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-        w4_few_kernel<T, ASYM, GPB, ML, NT, W, U, VEC><<<dim3((unsigned)blocks), W * 64, 0, stream>>>(p);
+        dim3 grid;
+        const hipError_t e = grid_of((p.g.nt + NT - 1) / NT, W * 64, &grid);
+        if (e != hipSuccess) return e;
+        w4_few_kernel<T, ASYM, GPB, ML, NT, W, U, VEC><<<grid, W * 64, 0, stream>>>(p);
         return hipGetLastError();
     };
     const auto tile = [&](auto mt, auto nt, auto ks) {
         constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, KS = decltype(ks)::value;
-        const int64_t blocks = ((p.m + 16 * MT - 1) / (16 * MT)) * ((p.g.nt + 4 * NT - 1) / (4 * NT));
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-        w4_tile_kernel<T, ASYM, GPB, MT, NT, KS, VEC><<<dim3((unsigned)blocks), 256 * KS, 0, stream>>>(p);
+        dim3 grid;
+        const hipError_t e = grid_of(((p.m + 16 * MT - 1) / (16 * MT)) * ((p.g.nt + 4 * NT - 1) / (4 * NT)), 256 * KS, &grid);
+        if (e != hipSuccess) return e;
+        w4_tile_kernel<T, ASYM, GPB, MT, NT, KS, VEC><<<grid, 256 * KS, 0, stream>>>(p);
         return hipGetLastError();
     };
     typedef std::integral_constant<int, 1> i1;

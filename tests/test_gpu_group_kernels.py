@@ -3,7 +3,7 @@ some of them do: products of binary32 operands in pieces, launches of 2^32 threa
 import numpy as np
 import pytest
 
-from test_gpu_groups import B, L, assert_within, make_w4, torch  # noqa: F401  (fixtures and helpers)
+from test_gpu_groups import B, L, assert_within, check_w4, make_w4, torch  # noqa: F401  (fixtures and helpers)
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,26 @@ def test_group_codes_past_a_launch(torch, L, B, rows, cols, group):
     halves_equal(torch, act, (y, aq, sa), rows, x)
     grad = lambda d, a, b: (L.ckpt_act_bwd(d, a, b, B.ACT_GELU, group=group),)
     halves_equal(torch, grad, grad(y, aq, sa), rows, y, aq, sa)
+
+
+def test_w4_past_a_launch(torch, L, B):
+    """512 threads for every 16 of 2^27 output columns, and for every 64 of 2^29 rows; a block
+    that fills up the last row of blocks stores nothing."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = (1 << 27) + 5
+    q = torch.randint(0, 256, (n, 1), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.rand(n, 1, generator=g, device="cuda")
+    x = torch.randn(2, 2, generator=g, device="cuda").bfloat16()
+    y = L.W4Linear(q, s, group=128)(x)
+    for part in (slice(0, n // 2), slice(n // 2, n)):
+        assert torch.equal(y[:, part], L.W4Linear(q[part], s[part], group=128)(x))
+    del q, s, y
+    rows = (1 << 29) + 5
+    x = torch.randn(rows, 2, generator=g, device="cuda", dtype=torch.float16)
+    lin = L.W4Linear(torch.full((1, 1), 0x2D, dtype=torch.uint8, device="cuda"), torch.full((1, 1), 0.75, device="cuda"),
+                     group=128, dtype=torch.float16)
+    buf = torch.full((rows + 1, 1), 7.0, device="cuda", dtype=torch.float16)
+    lin(x, out=buf[:rows])
+    assert buf[rows].item() == 7.0
+    halves_equal(torch, lambda v: (lin(v),), (buf[:rows],), rows, x)
+    check_w4(torch, buf[rows - 3:rows], x[-3:], torch.tensor([[-3.0 * 0.75, 2.0 * 0.75]], device="cuda"), None, 128, "last rows")
