@@ -236,6 +236,11 @@ __device__ __forceinline__ F spread(F v, int j) {
 // its x (1 x 8192 x 28672, f16 with zero points: 41.8 us with ML 16, 27.4 us with ML 4).
 //
 // GPB: scales per 128-K block and row (0: one per row, applied at the end).
+//
+// More blocks than a launch holds along x (2^32 threads) stand in rows of kFewRow.  (A row's
+// length from gridDim would be one more load to wait for: 1 x 4096 x 4096 3.7 us, so 3.6 us.)
+template <int W>
+constexpr int64_t kFewRow = 0xFFFFFFFFll / (W * 64);
 template <typename T, bool ASYM, int GPB, int ML, int NT, int W, int U, bool VEC>
 __global__ __launch_bounds__(W * 64) void w4_few_kernel(const W4Params p) {
     typedef typename Traits<T>::frag frag;
@@ -243,7 +248,8 @@ __global__ __launch_bounds__(W * 64) void w4_few_kernel(const W4Params p) {
     constexpr int C = 16 / ML, X = 4 / C, R = 4 / C;   // loads of x per block; accumulator registers of distinct rows
     __shared__ float red[W][NT][R * 64];
     const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, i = l & 15, g = l >> 4;
-    const int64_t t0 = block_id() * NT;   // a block past the end repeats the last rows and stores nothing
+    const int64_t t0 = (blockIdx.y * kFewRow<W> + blockIdx.x) * NT;
+    if (t0 >= p.g.nt) return;
     const uint4* codes[NT];
     const float* sc[NT];
     const uint8_t* zc[NT];
@@ -524,9 +530,8 @@ template <typename T, bool ASYM, int GPB, bool VEC>
 hipError_t launch_rows(const W4Params& p, hipStream_t stream) {
     const auto few = [&](auto ml, auto nt, auto w, auto u) {
         constexpr int ML = decltype(ml)::value, NT = decltype(nt)::value, W = decltype(w)::value, U = decltype(u)::value;
-        dim3 grid;
-        const hipError_t e = grid_of((p.g.nt + NT - 1) / NT, W * 64, &grid);
-        if (e != hipSuccess) return e;
+        const int64_t blocks = (p.g.nt + NT - 1) / NT, rows = (blocks + kFewRow<W> - 1) / kFewRow<W>;
+        const dim3 grid((unsigned)(rows == 1 ? blocks : kFewRow<W>), (unsigned)rows);
         w4_few_kernel<T, ASYM, GPB, ML, NT, W, U, VEC><<<grid, W * 64, 0, stream>>>(p);
         return hipGetLastError();
     };
