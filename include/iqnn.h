@@ -417,7 +417,9 @@ iqnn_status iqnn_maxpool2d(const void *x_dev, void *y_dev, int32_t n, int32_t h,
  * multiple, or 0 for one group per row.  scale and zp are [rows][G], G = ceil(cols /
  * group) (1 for group 0).  Outputs must not overlap inputs.  rows (m) = 0 is valid and,
  * but for iqnn_ckpt_wgrad, writes nothing.  Sizes: cols (n, k) at most 2^30, rows at most
- * 2^40, rows * ld at most 2^46 (IQNN_ERR_UNSUPPORTED). */
+ * 2^40, rows * ld at most 2^46; fewer than 2^31 blocks of 256 threads at one for 8 elements
+ * of a row (with group 0 at least 64 a row); a weight gradient of fewer than 2^24 tiles of
+ * 128 x 128 (IQNN_ERR_UNSUPPORTED). */
 
 /* Floating-point element types. */
 typedef enum {

@@ -69,7 +69,7 @@ iqnn_status check_wgrad(const iqnn_ckpt_wgrad_desc* d) {
         return fail(IQNN_ERR_INVALID_ARG, "ckpt_wgrad: dw_type %d is neither dy_type nor FLOAT32", d->dw_type);
     if (!group_ok(d->group)) return fail(IQNN_ERR_INVALID_ARG, "ckpt_wgrad: group %d is not 0, 32, 64 or 128", d->group);
     const WgradPlan w = wgrad_plan(d->m, d->n, d->k, d->dw_type == F_F32);
-    if (w.n_tiles * w.k_tiles * w.splits > 0x7FFFFFFF || (d->n * d->k + d->n) / 256 >= 0x7FFFFFFF)
+    if (w.n_tiles * w.k_tiles * w.splits > kWgradMaxBlocks)
         return fail(IQNN_ERR_UNSUPPORTED, "ckpt_wgrad: more blocks than a launch can hold");
     return IQNN_OK;
 }

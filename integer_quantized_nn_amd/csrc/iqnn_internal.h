@@ -290,6 +290,7 @@ struct WgradPlan {
     int64_t tile;             // 64 or 128, square
     int64_t n_tiles, k_tiles, splits, rows_per_split, workspace;
 };
+constexpr int64_t kWgradMaxBlocks = 0xFFFFFFFFll / 256;   // of 256 threads, below 2^32 in a launch
 WgradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, bool f32_out);
 
 struct WgradParams {

@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256 * KS, KS) void wgrad_kernel(const WgradParams p
     const int wn = (wave >> 1) * (BN / 2), wk = (wave & 1) * (BK / 2);
 
     const int64_t tiles = p.n_tiles * p.k_tiles;
-    const int64_t split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+    const int64_t id = block_id(), split = id / tiles, tile = id - split * tiles;
+    if (split >= p.splits) return;   // a block that fills up a row of blocks
     const int64_t n0 = (tile / p.k_tiles) * BN, k0 = (tile % p.k_tiles) * BK;
     const int64_t m_lo = split * p.rows_per_split;
     const int64_t m_hi = m_lo + p.rows_per_split < p.m ? m_lo + p.rows_per_split : p.m;
@@ -692,10 +693,13 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const WgradParams p) {
 
 template <typename T, bool SPLIT>
 hipError_t launch_mode(const WgradParams& p, hipStream_t stream) {
-    const dim3 g((unsigned)(p.n_tiles * p.k_tiles * p.splits));
+    const int64_t blocks = p.n_tiles * p.k_tiles * p.splits;
+    if (blocks > kWgradMaxBlocks) return hipErrorInvalidValue;
     const auto go = [&](auto fold, auto tile, auto sets) {
         constexpr bool F = decltype(fold)::value;
         constexpr int TILE = decltype(tile)::value, KS = decltype(sets)::value;
+        dim3 g;
+        grid_of(blocks, 256 * KS, &g);
         if (p.vec) wgrad_kernel<T, SPLIT, F, TILE, TILE, KS, true><<<g, 256 * KS, 0, stream>>>(p);
         else wgrad_kernel<T, SPLIT, F, TILE, TILE, KS, false><<<g, 256 * KS, 0, stream>>>(p);
     };
@@ -712,6 +716,7 @@ hipError_t launch_mode(const WgradParams& p, hipStream_t stream) {
     if constexpr (Mode<T, SPLIT>::pa == 1) {   // dY in one piece
         const auto ring = [&](auto sets) {
             constexpr int KS = decltype(sets)::value;
+            const dim3 g((unsigned)blocks);
             if (p.db) wgrad_ring_kernel<T, SPLIT, KS, true><<<g, 256 * KS, 0, stream>>>(p);
             else wgrad_ring_kernel<T, SPLIT, KS, false><<<g, 256 * KS, 0, stream>>>(p);
         };
@@ -726,7 +731,7 @@ hipError_t launch_mode(const WgradParams& p, hipStream_t stream) {
             // Two blocks on a CU overlap better than two sets of waves behind one barrier
             // (4096^3 bf16: 187-194 us against 207 us), if there is a second block for each CU
             // (12608 x 4096 x 1024, 256 blocks: 200 us against 143 us).
-            if (g.x > 256) ring(i1());
+            if (blocks > 256) ring(i1());
             else ring(i2());
         }
     } else {

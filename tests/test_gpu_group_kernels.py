@@ -158,3 +158,17 @@ def test_w4_past_a_launch(torch, L, B):
     assert buf[rows].item() == 7.0
     halves_equal(torch, lambda v: (lin(v),), (buf[:rows],), rows, x)
     check_w4(torch, buf[rows - 3:rows], x[-3:], torch.tensor([[-3.0 * 0.75, 2.0 * 0.75]], device="cuda"), None, 128, "last rows")
+
+
+def test_wgrad_past_a_launch(torch, L):
+    """512 threads for every 128 of 2^30 columns."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = 1 << 30
+    q = torch.randint(-127, 128, (1, k), generator=g, device="cuda", dtype=torch.int8)
+    s = torch.rand(1, k // 128, generator=g, device="cuda")
+    dy = torch.full((1, 1), 1.5, device="cuda", dtype=torch.bfloat16)
+    dw, db = L.ckpt_wgrad(dy, q, s, bias=True)
+    for part in (slice(0, k // 2), slice(k // 2, k)):
+        want, _ = L.ckpt_wgrad(dy, q[:, part], s[:, part.start // 128:part.stop // 128])
+        assert torch.equal(dw[:, part], want)
+    assert db.item() == 1.5 and dw[:, -1].item() != 0

@@ -155,3 +155,12 @@ def test_ckpt_wgrad_call_refusals():
     refused(INVALID, "null", B.iqnn_ckpt_wgrad, d, P, 128, P, P, P, None, None, size)
     refused(INVALID, "workspace", B.iqnn_ckpt_wgrad, d, P, 128, P, P, P, None, P, size - 1)
     refused(ALIGNMENT, "misaligned", B.iqnn_ckpt_wgrad, d, P, 128, P, P, P, None, P + 8, size)
+
+
+def test_ckpt_wgrad_tiles_of_a_launch():
+    """2^24 blocks of 256 threads are 2^32 threads, one more than a launch holds."""
+    assert B.iqnn_ckpt_wgrad_workspace(wg(m=1, n=2 ** 20 - 128, k=2 ** 18)) == 0
+    d = wg(m=1, n=2 ** 20, k=2 ** 18)
+    with pytest.raises(B.IqnnError, match="blocks"):
+        B.iqnn_ckpt_wgrad_workspace(d)
+    refused(UNSUPPORTED, "blocks", B.iqnn_ckpt_wgrad, d, P, d.n, P, P, P, P, P, 1 << 40)
