@@ -49,3 +49,19 @@ def test_linear_results_may_be_changed_in_place(shape):
     y.sum().backward()
     assert y.shape == shape[:-1] + (8,) and x.grad.shape == shape
     assert torch.all((x.grad.double() - 2 * w.double().sum(0)).abs() <= 10 * 2.0 ** -23 * 2 * w.double().abs().sum(0))
+
+
+def test_linear_makes_no_codes_without_a_gradient(monkeypatch):
+    """Evaluation of a trained layer quantizes nothing; with gradients on, it does."""
+    def quantize_groups(*args, **kw):
+        raise RuntimeError("codes made")
+
+    monkeypatch.setattr(L, "quantize_groups", quantize_groups)
+    x, w = torch.ones(3, 16), torch.ones(8, 16, requires_grad=True)
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            y = C.linear(x, w)
+        assert torch.equal(y, torch.full((3, 8), 16.0)) and not y.requires_grad
+    assert torch.equal(C.linear(x, w.detach()), torch.full((3, 8), 16.0))
+    with pytest.raises(RuntimeError, match="codes made"):
+        C.linear(x, w)
