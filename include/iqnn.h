@@ -482,7 +482,7 @@ iqnn_status iqnn_w4_fwd(const iqnn_w4_desc *desc, int64_t m, const void *x_dev, 
 /* Activation that keeps its input in 8 bits: y = act(x) from x itself, and in the same
  * pass the INT8 codes and scales of x as iqnn_quantize_groups.  gated: rows of x are [a |
  * b], 2 * cols wide (ldx >= 2 * cols), y = act(a) * b, and each half has its own groups:
- * q_dev [rows][2][cols], scale_dev [rows][2][G]. */
+ * q_dev [rows][2][cols], scale_dev [rows][2][G].  q_dev and scale_dev both NULL: y alone. */
 iqnn_status iqnn_ckpt_act_fwd(const void *x_dev, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
                               int32_t act, int gated, int32_t group, void *y_dev, int64_t ldy, void *q_dev,
                               float *scale_dev, void *stream);

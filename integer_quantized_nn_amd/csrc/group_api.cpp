@@ -166,7 +166,7 @@ iqnn_status iqnn_ckpt_act_fwd(const void* x_dev, int32_t x_type, int64_t rows, i
     if (s != IQNN_OK) return s;
     if (!is_act(act)) return fail(IQNN_ERR_INVALID_ARG, "%s: unknown activation %d", op, act);
     if (rows == 0) return ok();
-    if (!x_dev || !y_dev || !q_dev || !scale_dev) return fail(IQNN_ERR_INVALID_ARG, "%s: null pointer", op);
+    if (!x_dev || !y_dev || !q_dev != !scale_dev) return fail(IQNN_ERR_INVALID_ARG, "%s: null pointer", op);
     if (!aligned(x_dev, fsize(x_type)) || !aligned(y_dev, fsize(x_type)) || !aligned(scale_dev, 4))
         return fail(IQNN_ERR_ALIGNMENT, "%s: misaligned pointer", op);
     const bool vec = cols % 8 == 0 && rows_vec(x_dev, ldx, x_type) && rows_vec(y_dev, ldy, x_type) && aligned(q_dev, 8);

@@ -427,6 +427,7 @@ __global__ __launch_bounds__(256) void act_fwd_groups_kernel(const ActParams p) 
     if (GATED) merge_lanes<false>(rb, lanes);
     if (!in) return;
     act_chunk<T, GATED, VEC>(p, t.row, c0, n, a, b);
+    if (!p.q) return;   // y alone
     const int64_t halves = GATED ? 2 : 1;
     int64_t e = t.row * p.cols * halves + c0;
     int64_t g = t.row * p.groups * halves + t.u / lanes;
@@ -584,7 +585,7 @@ hipError_t launch_act_fwd(const ActParams& p, hipStream_t stream) {
         return with_bool(p.gated, [&](auto G) { return with_bool(p.vec, [&](auto V) {
             constexpr bool gt = decltype(G)::value, v = decltype(V)::value;
             dim3 g;
-            if (p.group) {
+            if (p.group || !p.q) {   // without codes no group matters
                 const hipError_t e = blocks_of(p.rows * p.units_per_row, &g);
                 if (e != hipSuccess) return e;
                 act_fwd_groups_kernel<T, gt, v><<<g, 256, 0, stream>>>(p);

@@ -236,7 +236,7 @@ struct GroupDequantParams {
 };
 hipError_t launch_dequantize_groups(const GroupDequantParams& p, hipStream_t stream);
 
-// Forward: x -> y, q, scale.  Backward: x is dy, y is dx, q and scale are read.  gated:
+// Forward: x -> y, q, scale (q nullptr: y alone).  Backward: x is dy, y is dx, q and scale are read.  gated:
 // x (dx) rows are [gate | up], 2 * cols wide, and codes and scales come in two halves.
 struct ActParams {
     const void* x;

@@ -397,25 +397,26 @@ class W4Linear:
         return y
 
 
-def ckpt_act(x, act, group=128, gated=False, out=None, stream=None):
+def ckpt_act(x, act, group=128, gated=False, out=None, stream=None, save=True):
     """(y, codes, scale): y = act(x), or act(a) * b with x = [a | b] when gated, and the
     8-bit codes and scales of x that ckpt_act_bwd reads, all from one pass over x.  No
-    gradient flows through it: checkpoint.act is the function that has one."""
+    gradient flows through it: checkpoint.act is the function that has one.  save=False: y
+    alone, codes and scale None."""
     rows, width, ft = _gpu(x, "x")
     _no_gradient(x, "ckpt_act (checkpoint.act has)")
     dev = x.device
     if _away(dev, stream):
         with _on(dev, stream, x, out):
-            return ckpt_act(x, act, group, gated, out)
+            return ckpt_act(x, act, group, gated, out, save=save)
     _need(not gated or width % 2 == 0, "a gated activation needs an even last axis")
     cols, lead = (width // 2 if gated else width), x.shape[:-1]
     g = groups_of(cols, group) * (2 if gated else 1)
     xr, ld = _rows(x, rows, width)
     y = _out(out, lead + (cols,), x.dtype, dev, x)
-    q = x.new_empty(lead + (width,), dtype=torch.int8)
-    s = x.new_empty(lead + (g,), dtype=torch.float32)
-    _done(B.lib().iqnn_ckpt_act_fwd(xr.data_ptr(), ft, rows, cols, ld, act, gated, group, y.data_ptr(), cols, q.data_ptr(),
-                                    s.data_ptr(), _current(dev)))
+    q = x.new_empty(lead + (width,), dtype=torch.int8) if save else None
+    s = x.new_empty(lead + (g,), dtype=torch.float32) if save else None
+    _done(B.lib().iqnn_ckpt_act_fwd(xr.data_ptr(), ft, rows, cols, ld, act, gated, group, y.data_ptr(), cols, _ptr(q),
+                                    _ptr(s), _current(dev)))
     return y, q, s
 
 

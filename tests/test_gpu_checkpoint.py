@@ -80,3 +80,30 @@ def test_gradients_are_not_dropped(torch, L, B):
             call(x)
             with pytest.raises(ValueError, match="gradient"):
                 call(forward_ad.make_dual(x, torch.ones_like(x)))
+
+
+def test_activation_without_gradient_keeps_no_codes(torch, L, B):
+    """Where no gradient can be asked for, checkpoint.act allocates its result and nothing
+    else, and gives the same values."""
+    from integer_quantized_nn_amd import checkpoint as C
+    for shape, group, gated in (((2048, 512), 128, False), ((2048, 512), 0, True), ((300, 6000), 0, False), ((33, 70), 32, True)):
+        for dt in (torch.bfloat16, torch.float32):
+            x = tokens(torch, *shape, dt, 1).cuda()
+            p = x.clone().requires_grad_()
+            want = C.act(p, B.ACT_SILU, group=group, gated=gated)
+            assert want.requires_grad
+
+            def check(v):
+                torch.cuda.synchronize()
+                torch.cuda.reset_peak_memory_stats()
+                before = torch.cuda.memory_stats()["requested_bytes.all.current"]
+                y = C.act(v, B.ACT_SILU, group=group, gated=gated)
+                assert torch.cuda.memory_stats()["requested_bytes.all.peak"] - before == y.numel() * y.element_size()
+                assert torch.equal(y, want) and not y.requires_grad
+
+            check(x)
+            for mode in (torch.no_grad, torch.inference_mode):
+                with mode():
+                    check(p)
+            y, q, s = L.ckpt_act(x, B.ACT_SILU, group=group, gated=gated, save=False)
+            assert q is None and s is None and torch.equal(y, want)

@@ -164,3 +164,12 @@ def test_ckpt_wgrad_tiles_of_a_launch():
     with pytest.raises(B.IqnnError, match="blocks"):
         B.iqnn_ckpt_wgrad_workspace(d)
     refused(UNSUPPORTED, "blocks", B.iqnn_ckpt_wgrad, d, P, d.n, P, P, P, P, P, 1 << 40)
+
+
+def test_ckpt_act_without_codes():
+    """Neither codes nor scales may come alone; the other checks stay."""
+    for bad, word in ((dict(x=0), "null"), (dict(y=0), "null"), (dict(s=P), "null"), (dict(q=P), "null"), (dict(y=P + 2), "misaligned"),
+                      (dict(group=96), "group"), (dict(kind=4), "activation")):
+        status = ALIGNMENT if word == "misaligned" else INVALID
+        refused(status, word, B.iqnn_ckpt_act_fwd, *act(**{"q": 0, "s": 0, **bad}))
+    B.iqnn_ckpt_act_fwd(*act(rows=0, x=0, y=0, q=0, s=0), stream=0)
