@@ -107,3 +107,30 @@ def test_activation_without_gradient_keeps_no_codes(torch, L, B):
                     check(p)
             y, q, s = L.ckpt_act(x, B.ACT_SILU, group=group, gated=gated, save=False)
             assert q is None and s is None and torch.equal(y, want)
+
+
+def test_mixed_types_under_autocast(torch, L, B):
+    """A 16-bit activation and a float32 weight, as mixed precision brings them: under autocast
+    all take its type, gradients come back in the leaves' own; outside it they are refused."""
+    from integer_quantized_nn_amd import checkpoint as C
+    w0, b0 = tokens(torch, 24, 64, torch.float32, 2).cuda(), tokens(torch, 1, 24, torch.float32, 4)[0].cuda()
+    for dt in (torch.bfloat16, torch.float16):
+        x0 = tokens(torch, 40, 64, dt, 1).cuda()
+        dy = tokens(torch, 40, 24, dt, 3).cuda()
+        x, w, b = (t.clone().requires_grad_() for t in (x0, w0, b0))
+        with torch.autocast("cuda", dtype=dt):
+            y = C.linear(x, w, b, group=32)
+        assert y.dtype == dt
+        y.backward(dy)
+        assert x.grad.dtype == dt and w.grad.dtype == torch.float32 and b.grad.dtype == torch.float32
+        xc, wc, bc = (t.to(dt).requires_grad_() for t in (x0, w0, b0))
+        yc = C.linear(xc, wc, bc, group=32)
+        yc.backward(dy)
+        assert torch.equal(y, yc) and torch.equal(x.grad, xc.grad)
+        assert torch.equal(w.grad, wc.grad.float()) and torch.equal(b.grad, bc.grad.float())
+        with torch.autocast("cuda", dtype=dt):      # only the bias differs; a type that none of them has
+            assert C.linear(x0, w0.to(dt), b0).dtype == dt
+            with pytest.raises(ValueError):
+                C.linear(x0, w0.double())
+        with pytest.raises(ValueError):
+            C.linear(x0, w0)
