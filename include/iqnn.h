@@ -509,10 +509,13 @@ size_t iqnn_ckpt_wgrad_workspace(const iqnn_ckpt_wgrad_desc *desc);
 
 /* dw_dev [n][k] and db_dev [n] (NULL for none) are overwritten, with zeros when m = 0.
  * 16-bit dw_type: x^ enters the products rounded to dy_type (for F16 its magnitude must
- * not exceed 65504, as of the f16 tensor it was), summation in binary32.  FLOAT32:
- * binary32 products of dY with x^, or, for F32 and F16 dY where group is 0 or a multiple of
- * 64, of dY * S with the codes (dY * S must be finite in binary32 then).  The order of
- * summation depends on the descriptor only.
+ * not exceed 65504, as of the f16 tensor it was), summation in binary32.  FLOAT32: products
+ * of dY with x^, each within 2^-23 of its value; or, for F32 and F16 dY where group is 0 or a
+ * multiple of the output tile's width, of dY * S rounded to binary32 with the codes, exact.
+ * The sizes select a tile of 64 or 128, so dY * S must be finite in binary32 where group is
+ * 0, 64 or 128.  The order of summation depends on the descriptor and on whether the rows of
+ * dY and of the codes are aligned in whole vectors, on nothing else: equal calls give equal
+ * results, a view of dY may differ from its contiguous copy in the last bits.
  * Non-finite dY or scales give non-finite results.  workspace_dev: 16-byte aligned. */
 iqnn_status iqnn_ckpt_wgrad(const iqnn_ckpt_wgrad_desc *desc, const void *dy_dev, int64_t lddy, const void *q_dev,
                             const float *scale_dev, void *dw_dev, void *db_dev, void *workspace_dev,
