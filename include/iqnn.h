@@ -534,6 +534,12 @@ iqnn_status iqnn_ckpt_wgrad(const iqnn_ckpt_wgrad_desc *desc, const void *dy_dev
 iqnn_status iqnn_probe_empty(void *stream);
 iqnn_status iqnn_probe_mfma_rate(int32_t iters, int32_t blocks, int32_t *sink_dev, void *stream);
 
+/* The kernel that iqnn_w4_fwd runs for m > 0 rows of x (aligned: in whole vectors), as four
+ * numbers: 0 and the rows it takes (4, 8, 16), 16-row tiles of weights per block and blocks of
+ * K in flight; or 1 and its tile's rows / 16, columns / 64 and sets of four waves.  Host only;
+ * for tests and profiles to see that they reach every kernel. */
+iqnn_status iqnn_w4_kernel(const iqnn_w4_desc *desc, int64_t m, int aligned, int32_t kernel[4]);
+
 #ifdef __cplusplus
 }
 #endif

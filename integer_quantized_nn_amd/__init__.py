@@ -12,5 +12,5 @@ from .binding import (  # noqa: F401
     iqnn_qgemm_prepack, iqnn_qgemm_prepack_host,
     iqnn_quantize, iqnn_quantize_pad,
     iqnn_ckpt_act_bwd, iqnn_ckpt_act_fwd, iqnn_ckpt_wgrad, iqnn_ckpt_wgrad_workspace, iqnn_dequantize_groups,
-    iqnn_quantize_groups, iqnn_w4_fwd, iqnn_w4_packed_size, iqnn_w4_prepack,
+    iqnn_quantize_groups, iqnn_w4_fwd, iqnn_w4_kernel, iqnn_w4_packed_size, iqnn_w4_prepack,
 )

@@ -108,6 +108,7 @@ def lib():
         "iqnn_w4_packed_size": (SZ, [WD]),
         "iqnn_w4_prepack": (I, [WD, P, P, P, P, SZ, P]),
         "iqnn_w4_fwd": (I, [WD, I64, P, I64, P, P, P, I64, P]),
+        "iqnn_w4_kernel": (I, [WD, I64, I, ctypes.POINTER(ctypes.c_int32)]),
         "iqnn_ckpt_act_fwd": (I, [P, I32, I64, I64, I64, I32, I, I32, P, I64, P, P, P]),
         "iqnn_ckpt_act_bwd": (I, [P, I32, I64, I64, I64, I32, I, I32, P, P, P, I64, P]),
         "iqnn_ckpt_wgrad_workspace": (SZ, [GW]),
@@ -303,6 +304,13 @@ def iqnn_w4_prepack(desc, q, scale, zp, packed, stream=None):
 def iqnn_w4_fwd(desc, m, x, ldx, packed, bias, y, ldy, stream=None):
     _check(lib().iqnn_w4_fwd(ctypes.byref(desc), m, _dev(x), ldx, _dev(packed), _dev(bias), _dev(y), ldy,
                              _stream(stream, y)))
+
+
+def iqnn_w4_kernel(desc, m, aligned=True):
+    """(tile, rows, nt, sets) of the kernel iqnn_w4_fwd runs for m rows of x."""
+    kernel = (ctypes.c_int32 * 4)()
+    _check(lib().iqnn_w4_kernel(ctypes.byref(desc), m, int(aligned), kernel))
+    return tuple(kernel)
 
 
 def iqnn_ckpt_act_fwd(x, x_type, rows, cols, ldx, act, gated, group, y, ldy, q, scale, stream=None):

@@ -156,6 +156,19 @@ iqnn_status iqnn_w4_fwd(const iqnn_w4_desc* desc, int64_t m, const void* x_dev, 
     return launched("w4_fwd", launch_w4(p, desc->x_type, zp, static_cast<hipStream_t>(stream)));
 }
 
+iqnn_status iqnn_w4_kernel(const iqnn_w4_desc* desc, int64_t m, int aligned_x, int32_t kernel[4]) {
+    const iqnn_status s = check_w4(desc);
+    if (s != IQNN_OK) return s;
+    if (m <= 0 || !kernel) return fail(IQNN_ERR_INVALID_ARG, "w4_kernel: m must be positive, kernel not null");
+    const W4Choice c = w4_choice(m, desc->n, w4_geom(desc->n, desc->k, desc->group, false).gpb, desc->x_type == F_F32,
+                                 aligned_x && desc->k % 8 == 0);
+    kernel[0] = c.tile;
+    kernel[1] = c.rows;
+    kernel[2] = c.nt;
+    kernel[3] = c.sets;
+    return ok();
+}
+
 iqnn_status iqnn_ckpt_act_fwd(const void* x_dev, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
                               int32_t act, int gated, int32_t group, void* y_dev, int64_t ldy, void* q_dev,
                               float* scale_dev, void* stream) {

@@ -272,6 +272,15 @@ struct W4PrepackParams {
 };
 hipError_t launch_w4_prepack(const W4PrepackParams& p, hipStream_t stream);
 
+// The kernel for m rows of x: of few rows (tile false; rows: 4, 8 or 16 of them, nt 16-row
+// tiles of weights a block, sets: blocks of K a wave has in flight) or of tiles (16 * rows x
+// 64 * nt, sets of four waves).  gpb: W4Geom's; vec: W4Params'.
+struct W4Choice {
+    bool tile;
+    int32_t rows, nt, sets;
+};
+W4Choice w4_choice(int64_t m, int64_t n, int32_t gpb, bool f32, bool vec);
+
 struct W4Params {
     const void* x;            // [m][ldx]
     const uint8_t* packed;

@@ -35,6 +35,41 @@ W4Geom w4_geom(int64_t n, int64_t k, int32_t group, bool zp) {
     return g;
 }
 
+W4Choice w4_choice(int64_t m, int64_t n, int32_t gpb, bool f32, bool vec) {
+    // Up to 16 rows: one 16-row tile of weights per block, unless there are so many that
+    // every CU has three; then four share each block's x where x is what costs (16 x 8192 x
+    // 28672 bf16: 34 us against 60 us; 16 x 4096 x 4096: 8.7 us against 6.7 us).
+    const bool wide = vec && (n + 15) / 16 >= 768;
+    if (m <= 4) {
+        if (!f32) return {false, 4, 1, 4};
+        return wide ? W4Choice{false, 4, 4, 1} : W4Choice{false, 4, 1, 2};
+    }
+    if (m <= 16) {
+        const int32_t rows = m <= 8 ? 8 : 16;
+        return wide ? W4Choice{false, rows, 4, 1} : W4Choice{false, rows, 1, 2};
+    }
+    // Tiles of 16 rows x 64 nt with sets of waves, by their measured time at K = 4096 per
+    // round of blocks that fill the 256 CUs (bf16, group 128): the fewest rounds of a tile
+    // that keeps its waves busy.
+    const auto rounds = [&](int64_t bm, int64_t bn, int64_t per_round) {
+        const int64_t blocks = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
+        return (blocks + per_round - 1) / per_round;
+    };
+    if (f32)   // three pieces of x: LDS holds 64 rows at most
+        return rounds(32, 64, 256) * 21 <= rounds(64, 128, 256) * 55 ? W4Choice{true, 2, 1, 2} : W4Choice{true, 4, 2, 1};
+    if (!vec)
+        return rounds(64, 64, 256) * 17 <= rounds(64, 128, 256) * 27 ? W4Choice{true, 4, 1, 2} : W4Choice{true, 4, 2, 2};
+    // the last one's sums of shorter groups do not fit beside its totals in 256 registers
+    const int tiles = gpb <= 1 ? 5 : 4;
+    const int64_t us[5] = {rounds(32, 64, 256) * 12, rounds(64, 64, 256) * 17, rounds(64, 128, 256) * 27,
+                           rounds(128, 128, 256) * 41, rounds(128, 128, 512) * 74};
+    const W4Choice of[5] = {{true, 2, 1, 4}, {true, 4, 1, 4}, {true, 4, 2, 2}, {true, 8, 2, 2}, {true, 8, 2, 1}};
+    int best = 0;
+    for (int i = 1; i < tiles; ++i)
+        if (us[i] < us[best]) best = i;
+    return of[best];
+}
+
 namespace {
 
 // Which K position (0..7 of a word) nibble i holds.  bf16 and f32 activations: v_cvt_off_f32_i4
@@ -548,53 +583,33 @@ hipError_t launch_rows(const W4Params& p, hipStream_t stream) {
     typedef std::integral_constant<int, 4> i4;
     typedef std::integral_constant<int, 8> i8;
     typedef std::integral_constant<int, 16> i16;
-    // Up to 16 rows: one 16-row tile of weights per block, unless there are so many that
-    // every CU has three; then four share each block's x where x is what costs (16 x 8192 x
-    // 28672 bf16: 34 us against 60 us; 16 x 4096 x 4096: 8.7 us against 6.7 us).
-    const bool wide = VEC && p.g.nt >= 768;
-    if (p.m <= 4) {
-        if constexpr (!std::is_same<T, float>::value) return few(i4(), i1(), i8(), i4());
-        else if (!wide) return few(i4(), i1(), i8(), i2());
-        else if constexpr (VEC) return few(i4(), i4(), i8(), i1());
-    }
-    if (p.m <= 8) {
-        if (!wide) return few(i8(), i1(), i8(), i2());
-        else if constexpr (VEC) return few(i8(), i4(), i8(), i1());
-    }
-    if (p.m <= 16) {
-        if (!wide) return few(i16(), i1(), i8(), i2());
-        else if constexpr (VEC) return few(i16(), i4(), i8(), i1());
-    }
-    // Tiles of 16 MT x 64 NT with KS sets of waves, by their measured time at K = 4096 per
-    // round of blocks that fill the 256 CUs (bf16, group 128): the fewest rounds of a tile
-    // that keeps its waves busy.
-    const auto rounds = [&](int64_t bm, int64_t bn, int64_t per_round) {
-        const int64_t blocks = ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn);
-        return (blocks + per_round - 1) / per_round;
-    };
-    if constexpr (std::is_same<T, float>::value) {
-        // three pieces of x: LDS holds 64 rows at most
-        return rounds(32, 64, 256) * 21 <= rounds(64, 128, 256) * 55 ? tile(i2(), i1(), i2()) : tile(i4(), i2(), i1());
-    } else if constexpr (!VEC) {
-        return rounds(64, 64, 256) * 17 <= rounds(64, 128, 256) * 27 ? tile(i4(), i1(), i2()) : tile(i4(), i2(), i2());
-    } else {
-        // the last one's sums of shorter groups do not fit beside its totals in 256 registers
-        constexpr int tiles = GPB <= 1 ? 5 : 4;
-        const int64_t us[5] = {rounds(32, 64, 256) * 12, rounds(64, 64, 256) * 17, rounds(64, 128, 256) * 27,
-                               rounds(128, 128, 256) * 41, rounds(128, 128, 512) * 74};
-        int best = 0;
-        for (int i = 1; i < tiles; ++i)
-            if (us[i] < us[best]) best = i;
-        switch (best) {
-        case 0: return tile(i2(), i1(), i4());
-        case 1: return tile(i4(), i1(), i4());
-        case 2: return tile(i4(), i2(), i2());
-        case 3: return tile(i8(), i2(), i2());
-        default:
-            if constexpr (tiles == 5) return tile(i8(), i2(), i1());
-            else return tile(i8(), i2(), i2());
+    constexpr bool F32 = std::is_same<T, float>::value;
+    const W4Choice c = w4_choice(p.m, p.n, GPB, F32, VEC);
+    if (!c.tile) {
+        if (c.rows == 4) {
+            if constexpr (!F32) return few(i4(), i1(), i8(), i4());
+            else if (c.nt == 1) return few(i4(), i1(), i8(), i2());
+            else if constexpr (VEC) return few(i4(), i4(), i8(), i1());
+        } else if (c.rows == 8) {
+            if (c.nt == 1) return few(i8(), i1(), i8(), i2());
+            else if constexpr (VEC) return few(i8(), i4(), i8(), i1());
+        } else {
+            if (c.nt == 1) return few(i16(), i1(), i8(), i2());
+            else if constexpr (VEC) return few(i16(), i4(), i8(), i1());
         }
+    } else if constexpr (F32) {
+        return c.rows == 2 ? tile(i2(), i1(), i2()) : tile(i4(), i2(), i1());
+    } else if constexpr (!VEC) {
+        return c.nt == 1 ? tile(i4(), i1(), i2()) : tile(i4(), i2(), i2());
+    } else {
+        if (c.rows == 2) return tile(i2(), i1(), i4());
+        if (c.rows == 4) return c.nt == 1 ? tile(i4(), i1(), i4()) : tile(i4(), i2(), i2());
+        if constexpr (GPB <= 1) {
+            if (c.sets == 1) return tile(i8(), i2(), i1());
+        }
+        return tile(i8(), i2(), i2());
     }
+    return hipErrorInvalidValue;   // no such form of w4_choice
 }
 
 template <typename T, bool ASYM>

@@ -3,7 +3,8 @@ some of them do: products of binary32 operands in pieces, launches of 2^32 threa
 import numpy as np
 import pytest
 
-from test_gpu_groups import B, L, assert_within, check_w4, make_w4, torch  # noqa: F401  (fixtures and helpers)
+from test_gpu_groups import (  # noqa: F401  (fixtures and helpers)
+    B, L, assert_within, check_w4, check_wgrad, make_codes, make_w4, tokens, torch)
 
 pytestmark = pytest.mark.gpu
 
@@ -107,6 +108,44 @@ def test_wgrad_pieces_of_the_largest_and_of_infinities(torch, L, dtype, n, k):
     s[r, 1] = float("inf")
     dw, _ = L.ckpt_wgrad(dy, q, s, group=32, out_dtype=torch.float32)
     assert not torch.isfinite(dw[:, 32:64]).any() and torch.isfinite(dw[:, :32]).all() and torch.isfinite(dw[:, 64:]).all()
+
+
+# ------------------------------------------------------------- every kernel choice
+
+# rows and output columns at which the choice falls on each kernel (K of them all 264 or 266,
+# which ends inside a block of 128): up to 4, 8 and 16 rows with few and many columns, then
+# tiles of 32 x 64, 64 x 64, 64 x 128, 128 x 128 and 128 x 128 two to a CU, and f32's 64 x 128
+W4_CHOICES = [(m, n) for m in (2, 4, 6, 8, 13, 16) for n in (77, 12293)] + [
+    (17, 70), (500, 2040), (509, 4090), (1020, 4090), (2035, 4089), (505, 2555)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("zp", [False, True])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("k", [264, 266])
+def test_w4_every_kernel(torch, L, B, dtype, zp, group, k):
+    dt = getattr(torch, dtype)
+    for n in sorted({n for _, n in W4_CHOICES}):
+        q, s, z, w = make_w4(torch, L, B, n, k, group, zp, n + group)
+        bias = tokens(torch, 1, n, dt, n)[0].cuda()
+        lin = L.W4Linear(q, s, z, group=group, bias=bias, dtype=dt)
+        for m in [m for m, nn in W4_CHOICES if nn == n]:
+            x = tokens(torch, m, k, dt, m).cuda()
+            y = lin(x)
+            check_w4(torch, y, x, w, bias, group, (m, n, k))
+            assert torch.equal(lin(x), y)
+
+
+@pytest.mark.parametrize("m,n,k,group", [(2049, 520, 1040, 32), (2090, 512, 1024, 0), (70, 2056, 2064, 64), (1, 2056, 2064, 128),
+                                         (33, 2200, 2024, 128), (257, 2058, 2050, 32), (257, 2058, 2050, 0), (96, 2048, 4096, 128)])
+def test_wgrad_f16_to_float_many_tiles(torch, L, B, m, n, k, group):
+    """Two pieces of dY, folded scales and not, in the larger tiles."""
+    q, s = make_codes(torch, L, B, m, k, group, m)
+    dy = tokens(torch, m, n, torch.float16, n).cuda()
+    dw, db = L.ckpt_wgrad(dy, q, s, group=group, out_dtype=torch.float32, bias=True)
+    check_wgrad(torch, dw, db, dy, q, s, group, (m, n, k))
+    again, none = L.ckpt_wgrad(dy, q, s, group=group, out_dtype=torch.float32)
+    assert none is None and torch.equal(again, dw)
 
 
 # ------------------------------------------------ launches of 2^32 threads and more

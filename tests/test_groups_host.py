@@ -173,3 +173,27 @@ def test_ckpt_act_without_codes():
         status = ALIGNMENT if word == "misaligned" else INVALID
         refused(status, word, B.iqnn_ckpt_act_fwd, *act(**{"q": 0, "s": 0, **bad}))
     B.iqnn_ckpt_act_fwd(*act(rows=0, x=0, y=0, q=0, s=0), stream=0)
+
+
+@pytest.mark.parametrize("x_type", [B.FLOAT32, B.FLOAT16, B.BFLOAT16])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("k", [264, 266])
+def test_gpu_tests_reach_every_w4_kernel(x_type, group, k):
+    """The sizes of the GPU test fall on every kernel that any size falls on."""
+    from test_gpu_group_kernels import W4_CHOICES
+    reached = {B.iqnn_w4_kernel(w4(n, k, x_type=x_type, group=group), m) for m, n in W4_CHOICES}
+    rows = list(range(1, 20)) + [2 ** i + d for i in range(5, 15) for d in (-1, 0, 1)]
+    cols = [1, 64, 300, 777] + [1024 * i + d for i in range(1, 40) for d in (-5, 0)]
+    every = {B.iqnn_w4_kernel(w4(n, k, x_type=x_type, group=group), m) for m in rows for n in cols}
+    assert reached == every
+    few = (3 if k % 8 else 5) + (x_type == B.FLOAT32 and k % 8 == 0)
+    tiles = 2 if k % 8 or x_type == B.FLOAT32 else 5 if group in (0, 128) else 4
+    assert len(every) == few + tiles
+
+
+def test_w4_kernel_refusals():
+    for d, m in ((w4(group=48), 1), (w4(), 0)):
+        with pytest.raises(B.IqnnError):
+            B.iqnn_w4_kernel(d, m)
+    # rows that are not aligned in whole vectors fall where an odd K falls
+    assert B.iqnn_w4_kernel(w4(4096, 4096), 2048, aligned=False) == B.iqnn_w4_kernel(w4(4096, 4094), 2048)
