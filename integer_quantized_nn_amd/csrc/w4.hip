@@ -38,7 +38,7 @@ W4Geom w4_geom(int64_t n, int64_t k, int32_t group, bool zp) {
 W4Choice w4_choice(int64_t m, int64_t n, int32_t gpb, bool f32, bool vec) {
     // Up to 16 rows: one 16-row tile of weights per block, unless there are so many that
     // every CU has three; then four share each block's x where x is what costs (16 x 8192 x
-    // 28672 bf16: 34 us against 60 us; 16 x 4096 x 4096: 8.7 us against 6.7 us).
+    // 28672 bf16: 36 us against 61 us; 16 x 4096 x 4096: 9.0 us against 6.9 us).
     const bool wide = vec && (n + 15) / 16 >= 768;
     if (m <= 4) {
         if (!f32) return {false, 4, 1, 4};
@@ -268,7 +268,7 @@ __device__ __forceinline__ F spread(F v, int j) {
 // operand, C = 16 / ML, and lane i loads step i % C of every C steps of row i / C: one load
 // brings C steps, which spread() hands to the C lanes of the row one by one.  With ML 4 a
 // 128-K block of x is one instruction instead of four, and the kernel no longer waits for
-// its x (1 x 8192 x 28672, f16 with zero points: 41.8 us with ML 16, 27.4 us with ML 4).
+// its x (1 x 8192 x 28672, f16 with zero points: 39.4 us with ML 16, 28.5 us with ML 4).
 //
 // GPB: scales per 128-K block and row (0: one per row, applied at the end).
 //

@@ -26,6 +26,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 //   HALF   bf16 or f16 gradients of bf16 or f16 dY: dY as it is, x^ rounded once to its
 //          type -- the activation as it was before it was saved, up to the code's own
 //          half step (2^-8 of the group's maximum; the rounding is 2^-9 or 2^-12 of x^).
+//          12608 x 4096 x 1024 bf16 lies 0.0022 from 64-bit sums (relative, root mean square),
+//          0.0017 of it the result's own rounding.  A second piece of x^ would double the
+//          products of a kernel whose products alone take half its time.
 //   SPLIT  f32 gradients: both operands as exact sums of bf16 pieces of 8 significand
 //          bits (dY 1, 2 or 3 of them, x^ 3); products of pieces i + j < 3 are kept.  Where
 //          that leaves any out, pieces are rounded to nearest: piece 1 is at most 2^-8 of the
@@ -371,15 +374,16 @@ __device__ __forceinline__ void load_lds4(uint8_t* lds, const void* src) {
 // one buffer of x^, two barriers, loads two stages ahead.)  KS sets of 2 x 2 waves take every
 // KS-th stage each, with LDS of their own, and add up at the end.
 //
-// What bounds it: 12608 x 4096 x 1024 bf16 takes 155 us, and copies of the kernel with a part
-// left out take 107 us without reading and restoring the codes, 125 without the direct loads
-// (137 without dY's, 141 without the codes' and scales'), 129 without the operand reads, 63
-// with products and barriers alone.  The parts overlap, so these do not add up.
+// What bounds it: 12608 x 4096 x 1024 bf16 takes 149 us, and copies of the kernel with a part
+// left out of its stages take 117 us without reading and restoring the codes, 117 without the
+// direct loads (132 without dY's, 138 without the codes' and scales'), 132 without the operand
+// reads, 70 with products and barriers alone.  The parts overlap, so these do not add up.
 //
 // The waits are counted here: the compiler would empty the queue before every transposed
 // read, and before every use of a code that came through a register (12608 x 4096 x 1024 bf16
-// so: 180 us).  Each stage requests the same four loads per wave, also behind the last row,
-// which is read again; so a batch has landed when at most the two later ones are outstanding.
+// so: 180 us, 164 us with the first counted waits).  Each stage requests the same four loads
+// per wave, also behind the last row, which is read again; so a batch has landed when at most
+// the two later ones are outstanding.
 //
 // The bias gradient rides on dY's fragments: a product with rows of ones.  Its eight 16-wide
 // column tiles are shared out among the waves and the blocks of a row of tiles, for a wave
@@ -729,8 +733,8 @@ hipError_t launch_mode(const WgradParams& p, hipStream_t stream) {
             ring(i1());
         } else {
             // Two blocks on a CU overlap better than two sets of waves behind one barrier
-            // (4096^3 bf16: 187-194 us against 207 us), if there is a second block for each CU
-            // (12608 x 4096 x 1024, 256 blocks: 200 us against 143 us).
+            // (4096^3 bf16: 186 us against 199 us), if there is a second block for each CU
+            // (12608 x 4096 x 1024, 256 blocks: 198 us against 149 us).
             if (blocks > 256) ring(i1());
             else ring(i2());
         }
@@ -761,8 +765,8 @@ WgradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, bool f32_out) {
     w.n_tiles = (n + w.tile - 1) / w.tile;
     w.k_tiles = (k + w.tile - 1) / w.tile;
     const int64_t tiles = w.n_tiles * w.k_tiles;
-    // (float results run two blocks on a CU: 256 tiles of 12608 x 4096 x 1024 bf16 take 405 us
-    // unsplit, 324 us split; 16-bit ones, one block of two sets of waves)
+    // (float results run two blocks on a CU: 256 tiles of 12608 x 4096 x 1024 bf16 take 402 us
+    // unsplit, 316 us split; 16-bit ones, one block of two sets of waves)
     int64_t s = tiles >= (f32_out ? 512 : 256) ? 1 : 512 / tiles;
     if (s > steps / 8) s = steps / 8;
     if (s < 1) s = 1;
