@@ -59,7 +59,7 @@ def test_wgrad_products_lean_to_no_side(torch, L, n, k):
 
 
 @pytest.mark.parametrize("zp", [False, True])
-@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("k", [264, 266])
 def test_w4_float_products_keep_every_piece(torch, L, B, zp, group, k):
     """One element of each row of x: y is one product x (q - z) S.  The three pieces' products
